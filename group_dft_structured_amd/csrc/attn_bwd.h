@@ -93,7 +93,8 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(BwdWave
   RowFrag<T, HD> of;
   of.load(a.o.data + (tok * a.o.ts + (int64_t)head * a.o.hs) * Tl::ES, c.dim, valid);
   const int64_t row_at = (int64_t)head * c.total_q + tok;
-  const float lse = valid ? a.lse[row_at] : -EQL_INF;
+  float lse = valid ? a.lse[row_at] : -EQL_INF;
+  if (lse == -EQL_INF) lse = EQL_INF;  // rows that saw nothing: every p is 2^-inf
 
   ScaledSum<T, HD> dq;
   dq.clear();
@@ -140,10 +141,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(BwdWave
     }
   }
 
-  float delta = 0.f, lse2 = EQL_INF;  // rows that saw nothing: every p is 2^-inf
-  // lse in base 2 is rounded; what is lost, a factor common to the row, goes into
-  // dp - delta (one fused operation either way), for the sums of ds in binary32
-  float fix = 1.f;
+  float delta = 0.f;
   {
 #pragma unroll
     for (int s = 0; s < Tl::STEPS; ++s) {
@@ -153,16 +151,9 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(BwdWave
       for (int e = 0; e < Tl::EPC; ++e) delta = __builtin_fmaf((float)x[e], (float)y[e], delta);
     }
     delta = pair_sum(delta);
-    if (__builtin_isfinite(lse)) {
-      lse2 = lse * LOG2E;
-      fix = __builtin_amdgcn_exp2f(-(__builtin_fmaf(lse, LOG2E, -lse2) + lse * LOG2E_LOW));
-    } else if (lse != -EQL_INF) {
-      lse2 = lse;
-    }
     if (valid && h == 0) a.delta[row_at] = delta;
   }
 
-  const float fixed_delta = delta * fix;
   if (HD == 128 && t1 > 0) fetch(0);
 
   for (int t = 0; t < t1; ++t) {
@@ -193,9 +184,9 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(BwdWave
         if (side != 0) {
           const float b = lut[side < 0 ? 0 : bw - 1];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) s[e] = __builtin_fmaf(s[e], c.scale2, b);
+          for (int e = 0; e < 16; ++e) s[e] = __builtin_fmaf(s[e], c.scale, b);
         } else if constexpr (BIAS == BIAS_INDEX) {
-          add_bias_row<1>(s, c.scale2, lut + (key0 + 32 * kb + 4 * h - pq + c.span + PAD));
+          add_bias_row<1>(s, c.scale, lut + (key0 + 32 * kb + 4 * h - pq + c.span + PAD));
         } else {
 #pragma unroll
           for (int e4 = 0; e4 < 4; ++e4) {
@@ -203,14 +194,13 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(BwdWave
 #pragma unroll
             for (int e = 0; e < 4; ++e) off[4 * e4 + e] = pk[e] - pq + c.span;
           }
-          add_bias_offsets(s, c.scale2, lut, off, width);
+          add_bias_offsets(s, c.scale, lut, off, width);
         }
       } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[e] *= c.scale2;
+        scale_scores(s, c.scale);
       }
 #pragma unroll
-      for (int e = 0; e < 16; ++e) dp[e] = __builtin_amdgcn_exp2f(s[e] - lse2) * __builtin_fmaf(dp[e], fix, -fixed_delta);
+      for (int e = 0; e < 16; ++e) dp[e] = __builtin_amdgcn_exp2f((s[e] - lse) * LOG2E) * (dp[e] - delta);
       if (key0 + BN > wmin) {
 #pragma unroll
         for (int e = 0; e < 16; ++e)
@@ -336,7 +326,7 @@ __global__ __launch_bounds__(64 * KW * QW) __attribute__((amdgpu_waves_per_eu(HD
       if (first + (int)threadIdx.x < lq) {
         const int64_t at = (int64_t)head * c.total_q + t + threadIdx.x;
         const float v = a.lse[at];
-        if (v != -EQL_INF) lse_next = v * LOG2E - SHIFT;
+        if (v != -EQL_INF) lse_next = v;
         delta_next = a.delta[at];
         if constexpr (BIAS == BIAS_POSITIONS) pos_next = c.pos_q[t + threadIdx.x];
       }
@@ -384,9 +374,9 @@ __global__ __launch_bounds__(64 * KW * QW) __attribute__((amdgpu_waves_per_eu(HD
         if (kw + 31 - (first + shift) <= -c.span || kw - (first + 31 + shift) >= c.span) {
           const float b = lut[kw < first + shift ? 0 : bw - 1];
 #pragma unroll
-          for (int e = 0; e < 16; ++e) s[e] = __builtin_fmaf(s[e], c.scale2, b);
+          for (int e = 0; e < 16; ++e) s[e] = __builtin_fmaf(s[e], c.scale, b);
         } else {
-          add_bias_row<-1>(s, c.scale2, lut + (pk - (first + 4 * h + shift) + c.span + PAD));
+          add_bias_row<-1>(s, c.scale, lut + (pk - (first + 4 * h + shift) + c.span + PAD));
         }
       } else if constexpr (BIAS == BIAS_POSITIONS) {
         int off[16];
@@ -396,10 +386,9 @@ __global__ __launch_bounds__(64 * KW * QW) __attribute__((amdgpu_waves_per_eu(HD
 #pragma unroll
           for (int e = 0; e < 4; ++e) off[4 * e4 + e] = pk - pq[e] + c.span;
         }
-        add_bias_offsets(s, c.scale2, lut, off, 2 * c.span + 1);
+        add_bias_offsets(s, c.scale, lut, off, 2 * c.span + 1);
       } else {
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[e] *= c.scale2;
+        scale_scores(s, c.scale);
       }
 #pragma unroll
       for (int e4 = 0; e4 < 4; ++e4) {
@@ -408,7 +397,7 @@ __global__ __launch_bounds__(64 * KW * QW) __attribute__((amdgpu_waves_per_eu(HD
         const floatx4 d4 = *reinterpret_cast<const floatx4*>(row_delta + r);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[4 * e4 + e] = __builtin_amdgcn_exp2f(s[4 * e4 + e] - l4[e]);
+          s[4 * e4 + e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[4 * e4 + e] - l4[e], LOG2E, SHIFT));
           dp[4 * e4 + e] = s[4 * e4 + e] * (dp[4 * e4 + e] - d4[e]);
         }
       }

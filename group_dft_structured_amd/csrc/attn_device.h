@@ -27,8 +27,11 @@ typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
 typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
+// Scores, their maxima and lse are kept in base e, and only differences of them go
+// to base 2: a score and a maximum of the same size then cancel exactly.  (lse times
+// log2 e is off by half a unit of its own last place, which at 10^9, a usual mask
+// value, is 2^6 in the exponent: gradients of infinity, or of zero.)
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
-constexpr float LOG2E_LOW = 1.92596299e-8f;  // log2 e - LOG2E
 #define EQL_INF __builtin_inff()
 
 enum { BIAS_NONE = 0, BIAS_INDEX = 1, BIAS_POSITIONS = 2 };
@@ -354,9 +357,7 @@ __host__ __device__ constexpr int bias_width(int span) {
   return 2 * span + 1 + (BIAS == BIAS_INDEX ? 2 * PAD : 0);
 }
 
-// The bias of every offset for heads head0 .. head0 + n - 1, in base 2.  A finite
-// table value stays finite (the lowest binary32 times log2 e would become an
-// infinity, which means that the offset is masked).
+// The bias of every offset for heads head0 .. head0 + n - 1.
 // Four offsets a thread at a time: the buckets of all four, then their values head by
 // head, are on their way together.  (One value after the other, bucket and then value,
 // took half of a new token's pass over a cache of 32768 with four heads of 257 offsets
@@ -379,33 +380,39 @@ __device__ __forceinline__ void fill_bias(float* lut, const Common& c, int head0
 #pragma unroll
       for (int u = 0; u < 4; ++u) t[u] = (float)from[u][g];
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        float v = t[u] * LOG2E;
-        if (__builtin_isfinite(t[u])) v = fminf(fmaxf(v, -1e38f), 1e38f);
-        if (i0 + u * threads < width) lut[g * width + i0 + u * threads] = in[u] ? v : 0.f;
-      }
+      for (int u = 0; u < 4; ++u)
+        if (i0 + u * threads < width) lut[g * width + i0 + u * threads] = in[u] ? t[u] : 0.f;
     }
   }
 }
 
-// Scores of a block to base 2, with the bias of the lane's row of offsets: INDEX,
+// Scores of a block, scaled, each rounded before a maximum or lse is taken from it:
+// merged with that into one operation, a score of 10^9 would differ from itself by up
+// to 2^5.
+__device__ __forceinline__ void scale_scores(floatx16& s, float scale) {
+#pragma clang fp contract(off)
+#pragma unroll
+  for (int e = 0; e < 16; ++e) s[e] = s[e] * scale;
+}
+
+// Scores of a block, scaled, with the bias of the lane's row of offsets: INDEX,
 // at[e] for result row 8 (e / 4) + e % 4 above the lane's first (at: PAD included;
 // step -1 where rows are queries); POSITIONS, offsets off.
 template <int STEP>
-__device__ __forceinline__ void add_bias_row(floatx16& s, float scale2, const float* at) {
+__device__ __forceinline__ void add_bias_row(floatx16& s, float scale, const float* at) {
   float b[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) b[e] = at[STEP * (8 * (e >> 2) + (e & 3))];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) s[e] = __builtin_fmaf(s[e], scale2, b[e]);
+  for (int e = 0; e < 16; ++e) s[e] = __builtin_fmaf(s[e], scale, b[e]);
 }
-__device__ __forceinline__ void add_bias_offsets(floatx16& s, float scale2, const float* lut,
+__device__ __forceinline__ void add_bias_offsets(floatx16& s, float scale, const float* lut,
                                                  const int (&off)[16], int width) {
   float b[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) b[e] = lut[clamp_int(off[e], 0, width - 1)];
 #pragma unroll
-  for (int e = 0; e < 16; ++e) s[e] = __builtin_fmaf(s[e], scale2, b[e]);
+  for (int e = 0; e < 16; ++e) s[e] = __builtin_fmaf(s[e], scale, b[e]);
 }
 
 // Values of a result column (d = 32 db + 8 g + 4 h + 0..3) to a row of the output.

@@ -3,12 +3,11 @@
 //
 // A work-group of NW waves takes 32 NW query rows of one sequence and head, each
 // wave 32 of them; keys and values go through LDS in tiles.  Per tile a wave
-// computes the scores transposed (keys x its 32 queries), takes them to base 2
-// with the scale and the bias, and multiplies exp2(score - maximum) from the
-// registers with the transposed values; a lane holds one query's column, so its
+// computes the scores transposed (keys x its 32 queries), adds the bias, and
+// multiplies exp(score - maximum) from the registers with the transposed values; a lane holds one query's column, so its
 // maximum and sum need one exchange between the two halves of the wave.
 //
-// The maximum moves only when a tile exceeds it by more than 2^8: until then the
+// The maximum moves only when a tile exceeds it by more than 8 ln 2: until then the
 // factors are at most 2^8 times 2^SHIFT and the output registers need no
 // rescaling.  SHIFT = 7 places binary16 factors in [.., 2^15]: the normal range
 // then reaches down to 2^-21 of the largest factor, and a rounding to 11 bits is
@@ -60,7 +59,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(FwdWave
   typedef Tile<T, HD> Tl;
   typedef FwdLds<T, HD, NW> Lds;
   constexpr int BN = Tl::ROWS, KB = Tl::BLOCKS, ROWS = 32 * NW, NT = 64 * NW;
-  constexpr float SHIFT = sizeof(T) == 2 ? 7.f : 0.f, SLACK = 8.f;
+  constexpr float SHIFT = sizeof(T) == 2 ? 7.f : 0.f, SLACK = 5.5f;  // below 8 ln 2
   extern __shared__ __attribute__((aligned(16))) char smem[];
   const Common& c = a.c;
   Where w;
@@ -161,12 +160,10 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(FwdWave
     for (int kb = 0; kb < KB; ++kb) s[kb] = mma_rows<T, HD>(tk, 32 * kb, qf, zero16());
     reads_ahead<KB * Reads<T, HD>::ROW, KB * Reads<T, HD>::ROW_MMA, 8>();
 
-    // base 2 scores with the bias
+    // scores with the bias
     if constexpr (BIAS == BIAS_NONE) {
 #pragma unroll
-      for (int kb = 0; kb < KB; ++kb)
-#pragma unroll
-        for (int e = 0; e < 16; ++e) s[kb][e] *= c.scale2;
+      for (int kb = 0; kb < KB; ++kb) scale_scores(s[kb], c.scale);
     } else {
       bool far = false;
       float fb = 0.f;
@@ -183,11 +180,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(FwdWave
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-          for (int e = 0; e < 16; ++e) s[kb][e] = __builtin_fmaf(s[kb][e], c.scale2, fb);
+          for (int e = 0; e < 16; ++e) s[kb][e] = __builtin_fmaf(s[kb][e], c.scale, fb);
       } else if constexpr (BIAS == BIAS_INDEX) {
         const float* at = lut_row + (key0 + 4 * h - pq + c.span + PAD);
 #pragma unroll
-        for (int kb = 0; kb < KB; ++kb) add_bias_row<1>(s[kb], c.scale2, at + 32 * kb);
+        for (int kb = 0; kb < KB; ++kb) add_bias_row<1>(s[kb], c.scale, at + 32 * kb);
       } else {
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
@@ -198,7 +195,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(FwdWave
 #pragma unroll
             for (int e = 0; e < 4; ++e) off[4 * e4 + e] = pk[e] - pq + c.span;
           }
-          add_bias_offsets(s[kb], c.scale2, lut_row, off, width);
+          add_bias_offsets(s[kb], c.scale, lut_row, off, width);
         }
       }
     }
@@ -218,7 +215,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(FwdWave
     top = pair_max(top);
     if (__any(top > m + SLACK)) {
       const float mn = fmaxf(m, top);
-      const float f = mn == -EQL_INF ? 1.f : __builtin_amdgcn_exp2f(m - mn);
+      const float f = mn == -EQL_INF ? 1.f : __builtin_amdgcn_exp2f((m - mn) * LOG2E);
       m = mn;
       l *= f;
 #pragma unroll
@@ -226,12 +223,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(FwdWave
 #pragma unroll
         for (int e = 0; e < 16; ++e) acc[db][e] *= f;
     }
-    const float base = (m == -EQL_INF ? 0.f : m) - SHIFT;  // nothing seen: every factor is 2^-inf
+    const float base = m == -EQL_INF ? 0.f : m;  // nothing seen: every factor is 2^-inf
 #pragma unroll
     for (int kb = 0; kb < KB; ++kb) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const float p = __builtin_amdgcn_exp2f(s[kb][e] - base);
+        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][e] - base, LOG2E, SHIFT));
         s[kb][e] = p;
         l += p;
       }
@@ -264,7 +261,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(FwdWave
     store_column<T, HD>(out + ((int64_t)token * a.o.ts + (int64_t)g * a.o.hs) * Tl::ES, acc, inv, c.dim);
   }
   if (a.lse != nullptr && valid && h == 0)
-    a.lse[out_row] = l == 0.f ? -EQL_INF : (m - SHIFT + __builtin_amdgcn_logf(l)) * LN2;
+    a.lse[out_row] = l == 0.f ? -EQL_INF : __builtin_fmaf(__builtin_amdgcn_logf(l) - SHIFT, LN2, m);
 }
 
 // Joins the splits of every row: a work-group a row.  A lane takes a split for
@@ -299,7 +296,7 @@ __global__ __launch_bounds__(256) void k_attn_join(const FwdArgs a, int max_q) {
   float l = 0.f;
 #pragma unroll
   for (int i = 0; i < MAX_SPLITS / 64; ++i) {
-    const float f = lv[i] == 0.f ? 0.f : __builtin_amdgcn_exp2f(mv[i] - base);  // 0: saw no key
+    const float f = lv[i] == 0.f ? 0.f : __builtin_amdgcn_exp2f((mv[i] - base) * LOG2E);  // 0: saw no key
     l = __builtin_fmaf(f, lv[i], l);
     if (wave == 0) weight[lane + 64 * i] = f;
   }
@@ -329,7 +326,7 @@ __global__ __launch_bounds__(256) void k_attn_join(const FwdArgs a, int max_q) {
     if (d < c.dim) out[d] = (T)((part[0][d] + part[1][d] + part[2][d] + part[3][d]) * inv);
   }
   if (a.lse != nullptr && lane == 0)
-    a.lse[row] = l == 0.f ? -EQL_INF : (m - SHIFT + __builtin_amdgcn_logf(l)) * LN2;
+    a.lse[row] = l == 0.f ? -EQL_INF : __builtin_fmaf(__builtin_amdgcn_logf(l) - SHIFT, LN2, m);
 }
 
 template <typename T, int HD, int NW, int BIAS>

@@ -60,6 +60,14 @@ struct SpanLoad {
   }
 };
 
+// Word l of `words` words from a uniform address, 0 behind them.  (Addresses of 64
+// bits a lane, kept over the loop, went to scratch memory, and their way back waited
+// for all loads of the next sequence: 198 us for 182 us.)
+__device__ __forceinline__ int lane_word(const void* from, int words, int tid) {
+  return __builtin_amdgcn_raw_buffer_load_b32(rows_of<float>(static_cast<const char*>(from), words, 1, 1),
+                                              (tid & 63) * 4, 0, 0);
+}
+
 // Offsets of the wave's scores (register e of block kb: key 32 kb + row(e, h), the
 // lane's query), for the bias and for the sums over offsets.
 template <int BIAS>
@@ -175,12 +183,12 @@ __global__ __launch_bounds__(128) __attribute__((amdgpu_waves_per_eu(HD * sizeof
       s[kb] = mma_rows<T, HD>(tk, 32 * kb, qf, zero16());
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        s[kb][e] = __builtin_fmaf(s[kb][e], c.scale2, bias[kb][e]);
+        s[kb][e] = __builtin_fmaf(s[kb][e], c.scale, bias[kb][e]);
         m = fmaxf(m, s[kb][e]);
       }
     }
     m = pair_max(m);
-    const float base = (m == -EQL_INF ? 0.f : m) - SHIFT;
+    const float base = m == -EQL_INF ? 0.f : m;
     floatx16 acc[HD / 32];
 #pragma unroll
     for (int db = 0; db < HD / 32; ++db) acc[db] = zero16();
@@ -188,7 +196,7 @@ __global__ __launch_bounds__(128) __attribute__((amdgpu_waves_per_eu(HD * sizeof
     for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        s[kb][e] = __builtin_amdgcn_exp2f(s[kb][e] - base);
+        s[kb][e] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[kb][e] - base, LOG2E, SHIFT));
         l += s[kb][e];
       }
       mma_cols<T, HD>(tv, 32 * kb, ColFrag<T>(s[kb]), acc);
@@ -201,7 +209,7 @@ __global__ __launch_bounds__(128) __attribute__((amdgpu_waves_per_eu(HD * sizeof
                       lq - 32 * wave, acc, inv, c.dim);
     if (a.lse != nullptr && valid && h == 0)
       a.lse[(int64_t)head * c.total_q + q0 + row] =
-          l == 0.f ? -EQL_INF : (m - SHIFT + __builtin_amdgcn_logf(l)) * LN2;
+          l == 0.f ? -EQL_INF : __builtin_fmaf(__builtin_amdgcn_logf(l) - SHIFT, LN2, m);
   }
 }
 
@@ -240,8 +248,7 @@ __global__ __launch_bounds__(128) __attribute__((amdgpu_waves_per_eu(HD * sizeof
   next.start(c, chunk);
   Span now = next.take(c);
   Stage<T, HD, 128, SHORT> sq, sd, so, sk, sv;
-  float lse_n = 0.f;
-  int pqn = 0, pkn = 0;
+  int lse_n = 0, pqn = 0, pkn = 0;
   auto fetch = [&](const Span& s, int tid) {
     const int64_t q0 = s.q0, k0 = s.k0;
     sq.load(a.q.data + (q0 * a.q.ts + (int64_t)head * a.q.hs) * Tl::ES, a.q.ts, s.nq(), c.dim, tid);
@@ -249,13 +256,10 @@ __global__ __launch_bounds__(128) __attribute__((amdgpu_waves_per_eu(HD * sizeof
     so.load(a.o.data + (q0 * a.o.ts + (int64_t)head * a.o.hs) * Tl::ES, a.o.ts, s.nq(), c.dim, tid);
     sk.load(a.k.data + (k0 * a.k.ts + (int64_t)head * a.k.hs) * Tl::ES, a.k.ts, s.nk(), c.dim, tid);
     sv.load(a.v.data + (k0 * a.v.ts + (int64_t)head * a.v.hs) * Tl::ES, a.v.ts, s.nk(), c.dim, tid);
-    lse_n = -EQL_INF;
-    if (lane < s.nq()) {
-      lse_n = a.lse[(int64_t)head * c.total_q + q0 + lane];
-      if constexpr (BIAS == BIAS_POSITIONS) pqn = c.pos_q[q0 + lane];
-    }
+    lse_n = lane_word(a.lse + (int64_t)head * c.total_q + q0, s.nq(), tid);
     if constexpr (BIAS == BIAS_POSITIONS) {
-      if (lane < s.nk()) pkn = c.pos_k[k0 + lane];
+      pqn = lane_word(c.pos_q + q0, s.nq(), tid);
+      pkn = lane_word(c.pos_k + k0, s.nk(), tid);
     }
   };
   fetch(now, threadIdx.x);
@@ -331,7 +335,7 @@ __global__ __launch_bounds__(128) __attribute__((amdgpu_waves_per_eu(HD * sizeof
         if (threadIdx.x % Tl::CPR == 0) row_delta[threadIdx.x / Tl::CPR + n * (128 / Tl::CPR)] = d;
       }
       if (wave == 0) {
-        row_lse[lane] = lse_n;
+        row_lse[lane] = lane < now.nq() ? __builtin_bit_cast(float, lse_n) : -EQL_INF;
         if constexpr (BIAS == BIAS_POSITIONS) {
           pos_k[lane] = pkn;
           pos_q[lane] = pqn;
@@ -362,13 +366,9 @@ __global__ __launch_bounds__(128) __attribute__((amdgpu_waves_per_eu(HD * sizeof
       RowFrag<T, HD> qf, df;
       qf.read(tq, 32 * wave, tid);
       df.read(td, 32 * wave, tid);
-      const float lse = row_lse[row], delta = row_delta[row];
-      float lse2 = lse == -EQL_INF ? EQL_INF : lse, fix = 1.f;
-      if (__builtin_isfinite(lse)) {  // as in the long pass
-        lse2 = lse * LOG2E;
-        fix = __builtin_amdgcn_exp2f(-(__builtin_fmaf(lse, LOG2E, -lse2) + lse * LOG2E_LOW));
-      }
-      const float fixed_delta = delta * fix;
+      const float delta = row_delta[row];
+      float lse = row_lse[row];
+      if (lse == -EQL_INF) lse = EQL_INF;  // rows that saw nothing: every p is 2^-inf
       floatx16 ds[2];
       float top = 0.f;
 #pragma unroll
@@ -377,8 +377,8 @@ __global__ __launch_bounds__(128) __attribute__((amdgpu_waves_per_eu(HD * sizeof
         ds[kb] = mma_rows<T, HD>(tv, 32 * kb, df, zero16(), tid);
 #pragma unroll
         for (int e = 0; e < 16; ++e) {
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(s[e], c.scale2, bias[kb][e]) - lse2);
-          ds[kb][e] = p * __builtin_fmaf(ds[kb][e], fix, -fixed_delta);
+          const float p = __builtin_amdgcn_exp2f((__builtin_fmaf(s[e], c.scale, bias[kb][e]) - lse) * LOG2E);
+          ds[kb][e] = p * (ds[kb][e] - delta);
           if constexpr (BIAS != BIAS_NONE) sums[kb][e] += ds[kb][e];
           if constexpr (sizeof(T) == 2) top = fmaxf(top, __builtin_fabsf(ds[kb][e]));
           s[e] = p * P_SCALE;

@@ -60,9 +60,10 @@ struct ScaledSum {
 // Whether two lanes of a half that count hold the same value.
 __device__ __forceinline__ bool repeats(int v, bool counts) {
   bool same = false;
+  const int tid = unknown_thread();  // or its 31 neighbours are kept, in scratch memory
 #pragma unroll
   for (int d = 1; d < 32; ++d) {
-    const int from = (threadIdx.x & 32) | ((threadIdx.x + d) & 31);
+    const int from = (tid & 32) | ((tid + d) & 31);
     same |= __shfl(v, from) == v && __shfl((int)counts, from) != 0;
   }
   return __any(same && counts);

@@ -83,7 +83,6 @@ void fill_common(Common* c, const eqattn_plan* p, const eqattn_packing_t* b, con
   c->buckets = p->buckets;
   c->span = p->span;
   c->scale = (float)p->scale;
-  c->scale2 = (float)(p->scale * 1.4426950408889634);
   c->seqs = (int)b->sequences;
   c->total_q = (int)b->total_q;
   c->total_k = (int)b->total_k;

@@ -26,7 +26,7 @@ struct View {
 struct Common {
   int H, Hk, G, dim, esize;  // G = H / Hk query heads share a key/value head
   int causal, buckets, span;
-  float scale, scale2;  // scale2 = scale * log2 e: scores are kept in base 2
+  float scale;
   int seqs, total_q, total_k, max_k;
   const int32_t *cu_q, *cu_k, *pos_q, *pos_k;
   const void* table;

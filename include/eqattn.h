@@ -35,7 +35,9 @@
  *     dv = p' do                     dtable[map[r], h] = sum of ds      (binary32)
  * where dk and dv also sum over the query heads that share a key/value head.
  *
- * Arithmetic.  Scores, softmax statistics, delta and every sum are binary32.  In
+ * Arithmetic.  Scores, softmax statistics, delta and every sum are binary32.  A
+ * finite table value of any size leaves results finite (beside it a score keeps
+ * what binary32 has room for).  In
  * binary16 plans the factors p and ds of the matrix products are rounded to
  * binary16, scaled by a power of two (per query or key) that keeps them in its
  * normal range; o, dq, dk and dv are rounded once.  Every sum has a fixed order,

@@ -1,0 +1,147 @@
+"""Attention on the GPU at values where a score, a sum or a scale can leave the
+range or the precision that its neighbours need.  The tolerances are those of
+test_gpu_attention.py (u = 2^-24; binary16 outputs and factors 2^-11) with the error
+of a score written out: a binary32 sum of dim products, (dim + 8) u times the
+largest product of norms, and one rounding of the sum with the bias, u of it."""
+import numpy as np
+import pytest
+
+from tests import plain64
+from tests.attn_cases import make
+from tests.gpu_helpers import gpu_available, to_np64, torch_mod
+from tests.test_gpu_attention import U, _backward, _forward, _plain, _within
+
+pytestmark = pytest.mark.gpu
+GRADS = ("dq", "dk", "dv", "dtable")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _need_gpu():
+    if not gpu_available():
+        pytest.skip("no GPU")
+
+
+def _products(c):
+    """Largest scaled sum of magnitudes of a score without its bias."""
+    q, k = c["q"].astype(np.float64), c["k"].astype(np.float64)
+    return c["scale"] * np.linalg.norm(q, axis=2).max() * np.linalg.norm(k, axis=2).max()
+
+
+def _check_grads(c, grads, ref, mag, relative, rows=None):
+    """relative: the error of a factor p, as a part of it."""
+    half = 2.0 ** -11 if c["dtype"] == "f16" else 0.0
+    group = c["H"] // c["Hk"]
+    n = {"dq": c["max_k"], "dk": c["max_q"] * group, "dv": c["max_q"] * group,
+         "dtable": 2 * (c["max_k"] + c["max_q"]) + 512}
+    for name, got, r, m in zip(GRADS, grads, ref, mag):
+        if r is None:
+            continue
+        h = 0.0 if name == "dtable" else half
+        bound = m * (h + relative + (n[name] + c["dim"] + 64) * U) + h * np.abs(r) + (2.0 ** -25 if h else 1e-30)
+        got = to_np64(got)
+        if rows is not None:
+            if name != "dq":
+                continue
+            got, r, bound = got[rows], r[rows], bound[rows]
+        _within(got, r, bound, name)
+
+
+# sequences of one tile and longer ones, offsets by index and by given positions
+LENGTHS = [([40, 64], "line"), ([40, 150], "line"), ([36, 49], "grid"), ([100, 169], "grid")]
+
+
+@pytest.mark.parametrize("lens,bias", LENGTHS)
+@pytest.mark.parametrize("value", [-1e4, -1e6, -1e9, -1.1e9, -3e9, -1e10, -7e15, -1e30, -3.4028235e38, 3e9])
+def test_a_large_bias_on_every_key_of_a_head(value, lens, bias, monkeypatch):
+    # the rows of the first head have nothing but the large value: finite, and a mask
+    # value that a program may well use.  A binary32 score near it is the value plus
+    # what of the product its last place keeps, and its factor is exp(score - lse).
+    c = make(lens, lens, 4, 4 if bias == "line" else 2, 32, "f32", False, bias, seed=8, grid=13)
+    c["table"][:, 0] = value
+    o, lse = _forward(c)
+    grads = _backward(c, o, lse)
+    torch_mod().cuda.synchronize()
+    assert bool(torch_mod().isfinite(o).all()) and bool(torch_mod().isfinite(lse).all())
+    for name, g in zip(GRADS, grads):
+        assert bool(torch_mod().isfinite(g).all()), name
+    # one rounding of each score, and for the row sums one of lse (which is given here)
+    error = (c["dim"] + 8) * U * _products(c) + U * (abs(value) + _products(c))
+    if abs(value) >= 1e9:  # half a last place is 32, more than any product: the score is the value
+        assert _products(c) < 32 and np.float32(value) == c["table"][0, 0]
+        error = (c["dim"] + 8) * U * _products(c)
+        exact = plain64.scores
+
+        def rounded(*a):
+            s, ids = exact(*a)
+            return np.where(np.isfinite(s) & (np.abs(s) > 1e8), np.float64(np.float32(s)), s), ids
+
+        monkeypatch.setattr(plain64, "scores", rounded)
+        same = np.float64(np.float32(value))
+        assert bool((lse[0].double() == same).all())
+    ref, mag = plain64.attention_backward(c, c["dout"], c["q"], c["k"], c["v"], to_np64(o), to_np64(lse),
+                                          **_plain(c))
+    # a factor is off by exp(error) - 1
+    _check_grads(c, grads, ref, mag, np.expm1(2 * error) + 16 * U)
+
+
+@pytest.mark.parametrize("lens,bias", LENGTHS)
+@pytest.mark.parametrize("value", [-1e6, -1e9, -3e9, -1e30, -3.4028235e38])
+def test_large_finite_biases_hide_offsets(value, lens, bias):
+    # every row sees other keys too: what is hidden has a factor of zero
+    c = make(lens, lens, 4, 4 if bias == "line" else 2, 32, "f32", False, bias, seed=9, grid=13)
+    if bias == "line":
+        c["table"][:5] = value
+    else:
+        c["table"][::2] = value
+        c["table"][len(c["table"]) // 2] = 0.5  # a token sees itself
+    ordinary = np.where(np.abs(c["table"]) > 1e5, 0, c["table"])
+    error = (c["dim"] + 8) * U * (_products(c) + np.abs(ordinary).max())
+    o, lse = _forward(c)
+    grads = _backward(c, o, lse)
+    torch_mod().cuda.synchronize()
+    ref, mag = plain64.attention_backward(c, c["dout"], c["q"], c["k"], c["v"], to_np64(o), to_np64(lse),
+                                          **_plain(c))
+    _check_grads(c, grads, ref, mag, 2 * error + 16 * U)
+
+
+@pytest.mark.parametrize("dtype,size", [("f16", 400.0), ("f32", 3e3), ("f32", 1e6)])
+@pytest.mark.parametrize("lens,Hk", [([40, 64], 4), ([40, 150], 2)])
+def test_scores_far_from_zero(lens, Hk, dtype, size):
+    # every row has a key that is its only one (the gap to the next is far above a
+    # score's last place): its factor is one, however large score and lse are
+    c = make(lens, lens, 4, Hk, 32, dtype, False, None, seed=10, std=size)
+    n, group = sum(lens), 4 // Hk
+    o, lse = _forward(c)
+    grads = _backward(c, o, lse)
+    torch_mod().cuda.synchronize()
+    half = 2.0 ** -11 if dtype == "f16" else 0.0
+    dv, dmag, count = np.zeros(c["v"].shape), np.zeros(c["v"].shape), np.zeros((n, Hk), int)
+    start = 0
+    clear = np.ones((n, 4), bool)
+    for length in lens:
+        at = slice(start, start + length)
+        for h in range(4):
+            s = c["q"][at, h].astype(np.float64) @ c["k"][at, h // group].astype(np.float64).T * c["scale"]
+            order = np.sort(s, axis=1)
+            best = start + s.argmax(axis=1)
+            clear[at, h] = order[:, -1] - order[:, -2] > 40 + 4 * (c["dim"] + 8) * U * _products(c)
+            np.add.at(dv[:, h // group], best, c["dout"][at, h].astype(np.float64))
+            np.add.at(dmag[:, h // group], best, np.abs(c["dout"][at, h].astype(np.float64)))
+            np.add.at(count[:, h // group], best, 1)
+            keep = clear[at, h]
+            _within(to_np64(o)[at, h][keep], c["v"][best, h // group].astype(np.float64)[keep],
+                    (half + 8 * U) * np.abs(c["v"][best, h // group].astype(np.float64)[keep]) + 1e-30, "o")
+        start += length
+    for g in grads[:3]:
+        assert bool(torch_mod().isfinite(g).all())
+    # a row whose two best keys are close leaves its sequence out of the comparison of
+    # dv; there are few of them, since a gap is of the size of the scores
+    assert clear.mean() > 0.95
+    start = 0
+    for length in lens:
+        at = slice(start, start + length)
+        for g in range(Hk):
+            if clear[at, g * group:(g + 1) * group].all():
+                bound = dmag[at, g] * (2 * half + (count[at, g].max() + 24) * U) + (2.0 ** -25 if half else 1e-30)
+                _within(to_np64(grads[2])[at, g], dv[at, g], bound, "dv")
+        start += length
