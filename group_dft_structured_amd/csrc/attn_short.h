@@ -388,9 +388,10 @@ __global__ __launch_bounds__(128) __attribute__((amdgpu_waves_per_eu(HD * sizeof
       // one power of two for the wave's 32 queries: ds of binary16 in 2^14 .. 2^15
       // at the largest, and normal down to 2^-28 of it
       if constexpr (sizeof(T) == 2) {
+        top = pair_max(top);
+        top = top < EQL_INF ? top : 0.f;  // a query of infinities has no say
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-        top = pair_max(top);
         scale = __builtin_ldexpf(1.f, clamp_int(15 - __builtin_amdgcn_frexp_expf(top), -100, 100));
       }
 #pragma unroll

@@ -145,3 +145,27 @@ def test_scores_far_from_zero(lens, Hk, dtype, size):
                 bound = dmag[at, g] * (2 * half + (count[at, g].max() + 24) * U) + (2.0 ** -25 if half else 1e-30)
                 _within(to_np64(grads[2])[at, g], dv[at, g], bound, "dv")
         start += length
+
+
+def _dq_reference(c, o, lse):
+    ref, mag = plain64.attention_backward(c, c["dout"], c["q"], c["k"], c["v"], to_np64(o), to_np64(lse),
+                                          **_plain(c))
+    error = (c["dim"] + 8) * U * (_products(c) + (0 if c["table"] is None else np.abs(c["table"]).max()))
+    return ref, mag, 2 * error + 16 * U
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("lens", [[40, 60], [40, 150]])
+@pytest.mark.parametrize("value", [np.inf, -np.inf, np.nan])
+def test_a_gradient_that_is_not_finite_stays_in_its_query(value, lens, dtype):
+    # (in dq; keys and values sum over all queries)
+    c = make(lens, lens, 2, 2, 32, dtype, False, "line", seed=11, do_std=40.0)
+    o, lse = _forward(c)
+    ref, mag, relative = _dq_reference(c, o, lse)
+    others = np.ones((sum(lens), 2), bool)
+    for token, head in ((5, 0), (33, 1), (sum(lens) - 1, 0)):
+        c["dout"][token, head, 3] = value
+        others[token, head] = False
+    grads = _backward(c, o, lse)
+    torch_mod().cuda.synchronize()
+    _check_grads(c, grads, ref, mag, relative, rows=others)
