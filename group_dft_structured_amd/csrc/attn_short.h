@@ -351,7 +351,7 @@ __global__ __launch_bounds__(128) __attribute__((amdgpu_waves_per_eu(HD * sizeof
 
     // ---- 32 queries a wave: dq, and ds for the bias ----
     floatx16 dq[HD / 32];
-    float scale = 1.f;
+    float scale = 1.f, own = 1.f;  // of ds, for dk and for dq
     if (wave * 32 < lq) {
       const bool valid = row < lq;
       const int pq = BIAS == BIAS_POSITIONS ? pos_q[row] : row + shift;
@@ -386,13 +386,18 @@ __global__ __launch_bounds__(128) __attribute__((amdgpu_waves_per_eu(HD * sizeof
         store_block(tp, kb, s, tid);
       }
       // one power of two for the wave's 32 queries: ds of binary16 in 2^14 .. 2^15
-      // at the largest, and normal down to 2^-28 of it
+      // at the largest, and normal down to 2^-28 of it, for dk; for dq a query whose
+      // own largest would be below 2 gets a power of its own
+      bool apart = false;
       if constexpr (sizeof(T) == 2) {
         top = pair_max(top);
         top = top < EQL_INF ? top : 0.f;  // a query of infinities has no say
+        const float mine = top;
 #pragma unroll
         for (int d = 1; d < 32; d *= 2) top = fmaxf(top, __shfl_xor(top, d));
-        scale = __builtin_ldexpf(1.f, clamp_int(15 - __builtin_amdgcn_frexp_expf(top), -100, 100));
+        scale = own = __builtin_ldexpf(1.f, clamp_int(15 - __builtin_amdgcn_frexp_expf(top), -100, 100));
+        apart = __any(mine > 0.f && mine * 0x1p13f < top);
+        if (apart) own = __builtin_ldexpf(1.f, clamp_int(15 - __builtin_amdgcn_frexp_expf(mine), -100, 100));
       }
 #pragma unroll
       for (int db = 0; db < HD / 32; ++db) dq[db] = zero16();
@@ -400,8 +405,14 @@ __global__ __launch_bounds__(128) __attribute__((amdgpu_waves_per_eu(HD * sizeof
       for (int kb = 0; kb < 2; ++kb) {
 #pragma unroll
         for (int e = 0; e < 16; ++e) ds[kb][e] *= scale;
-        const ColFrag<T> f(ds[kb]);
+        ColFrag<T> f(ds[kb]);
         store_block(ts, kb, ds[kb], tid);
+        if (apart) {
+          const float more = own / scale;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) ds[kb][e] *= more;
+          f = ColFrag<T>(ds[kb]);
+        }
         mma_cols<T, HD>(tk, 32 * kb, f, dq, tid);
       }
       if (lane == 0) ds_scale[wave] = scale;
@@ -411,7 +422,7 @@ __global__ __launch_bounds__(128) __attribute__((amdgpu_waves_per_eu(HD * sizeof
     char* rows = tk + wave * 32 * HD * Tl::ES;
     if (wave * 32 < lq)
       store_rows<T, HD>(rows, a.dq.data + ((q0 + 32 * wave) * a.dq.ts + (int64_t)head * a.dq.hs) * Tl::ES,
-                        a.dq.ts, lq - 32 * wave, dq, c.scale / scale, c.dim, tid);
+                        a.dq.ts, lq - 32 * wave, dq, c.scale / own, c.dim, tid);
 
     // ---- 32 keys a wave: dk and dv ----
     if (wave * 32 < lk) {

@@ -39,8 +39,10 @@
  * finite table value of any size leaves results finite (beside it a score keeps
  * what binary32 has room for).  In
  * binary16 plans the factors p and ds of the matrix products are rounded to
- * binary16, scaled by a power of two (per query or key) that keeps them in its
- * normal range; o, dq, dk and dv are rounded once.  Every sum has a fixed order,
+ * binary16, scaled by a power of two (per query for dq, per key for dk; for dk of
+ * sequences of at most 64 tokens per 32 queries, so that a key whose every ds is
+ * below 2^-28 of their largest loses digits) that keeps them in its normal range;
+ * o, dq, dk and dv are rounded once.  Every sum has a fixed order,
  * so the same call gives the same bits (dtable: where the positions of a
  * sequence's queries are distinct).  Sequences do not see each other's values,
  * infinities and NaN included.  Within a sequence a key or value that is not

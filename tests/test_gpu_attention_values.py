@@ -169,3 +169,24 @@ def test_a_gradient_that_is_not_finite_stays_in_its_query(value, lens, dtype):
     grads = _backward(c, o, lse)
     torch_mod().cuda.synchronize()
     _check_grads(c, grads, ref, mag, relative, rows=others)
+
+
+@pytest.mark.parametrize("lens", [[40, 60], [40, 150]])
+@pytest.mark.parametrize("ratio", [2.0 ** -14, 2.0 ** -22, 2.0 ** -32])
+def test_queries_with_small_gradients_beside_large_ones(ratio, lens):
+    # in binary16 a query's factors are scaled by its own size
+    c = make(lens, lens, 2, 2, 32, "f16", False, "line", seed=12, do_std=8000.0)
+    rows = np.arange(sum(lens)) % 5 != 0
+    c["dout"][rows] = (c["dout"][rows].astype(np.float64) * ratio).astype(np.float16)
+    # keys of 2^7 and queries of 2^-7: gradients of queries far above binary16's last place
+    c["q"] = (c["q"].astype(np.float64) / 128).astype(np.float16)
+    c["k"] = (c["k"].astype(np.float64) * 128).astype(np.float16)
+    c["dout"] = np.clip(c["dout"], -30000, 30000)
+    c["v"] = (c["v"].astype(np.float64) / 128).astype(np.float16)
+    o, lse = _forward(c)
+    ref, mag, relative = _dq_reference(c, o, lse)
+    grads = _backward(c, o, lse)
+    torch_mod().cuda.synchronize()
+    assert np.isfinite(to_np64(grads[0])).all()
+    everywhere = np.ones((sum(lens), 2), bool)
+    _check_grads(c, grads, ref, mag, relative, rows=everywhere)
