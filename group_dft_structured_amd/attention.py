@@ -6,7 +6,7 @@ import math
 from array import array
 
 from . import _DTYPE_CODE, EQL_F16, _check, _ptr, _stream, load_library
-from ._tensors import Launch, expect, expect_rows, expect_workspace, torch_dtype
+from ._tensors import Launch, expect, expect_rows, expect_workspace, refuse, torch_dtype
 
 ATTN_EXPORTED = (
     "eqattn_plan_create",
@@ -118,6 +118,8 @@ class Packing:
         """The fields of eqattn_packing_t for these token counts, tensors checked."""
         i32, dev = go.torch.int32, go.device
         rows = self.cu_q.shape
+        if len(rows) != 1 or rows[0] < 1:
+            refuse(self.cu_q, ("sequences + 1",), i32, dev, "contiguous ")
         cq = expect(self.cu_q, rows, i32, dev)
         ck = cq if self.cu_k is self.cu_q else expect(self.cu_k, rows, i32, dev)
         pq = 0 if self.pos_q is None else expect(self.pos_q, (total_q,), i32, dev)
