@@ -139,7 +139,7 @@ class AttnPlan:
     def __init__(self, heads, dim, kv_heads=None, dtype="f16", causal=False, scale=None, buckets=0,
                  span=0):
         self.handle = None
-        self.H, self.Hk, self.dim, self.dtype = heads, kv_heads or heads, dim, dtype
+        self.H, self.Hk, self.dim, self.dtype = heads, heads if kv_heads is None else kv_heads, dim, dtype
         self.causal, self.buckets, self.span = causal, buckets, span
         self.scale = 1.0 / math.sqrt(dim) if scale is None else scale
         self._dt = torch_dtype(dtype)

@@ -5,7 +5,7 @@ import types
 import pytest
 import torch
 
-from group_dft_structured_amd import Packing
+from group_dft_structured_amd import AttnPlan, EqlinearError, Packing
 
 GO = types.SimpleNamespace(torch=torch, device=-1)
 
@@ -39,3 +39,10 @@ def test_packing_refuses_other_lengths_and_types():
             Packing(cu, 4, bad, 4).fields(7, 7, GO)
     with pytest.raises(ValueError):
         Packing(cu, 4, pos_q=torch.zeros(6, dtype=torch.int32)).fields(7, 7, GO)
+
+
+def test_no_key_value_heads_are_refused():
+    with pytest.raises(EqlinearError, match="EQL_ERR_INVALID_ARG"):
+        AttnPlan(4, 64, kv_heads=0)
+    plan = AttnPlan(4, 64)
+    assert plan.Hk == 4
