@@ -1,7 +1,7 @@
 // C ABI of attention (include/eqattn.h): argument validation, the shapes of a
 // pass (waves, tiles, splits) and dispatch.  Every check runs before the first
 // HIP call.
-#include <math.h>
+#include <float.h>
 #include <string.h>
 
 #include <new>
@@ -216,7 +216,7 @@ eqlinear_status_t eqattn_plan_create(int64_t heads, int64_t kv_heads, int64_t di
   if (out == nullptr) return EQL_ERR_INVALID_ARG;
   *out = nullptr;
   if (heads <= 0 || kv_heads <= 0 || dim <= 0 || heads % kv_heads != 0) return EQL_ERR_INVALID_ARG;
-  if (!isfinite(scale) || !(scale > 0) || buckets < 0 || span < 0 || (buckets == 0 && span != 0))
+  if (!(scale > 0 && scale <= FLT_MAX) || buckets < 0 || span < 0 || (buckets == 0 && span != 0))
     return EQL_ERR_INVALID_ARG;
   const int dv = eql::enum_value(dtype_arg);
   if (dv != EQL_F32 && dv != EQL_F16) return EQL_ERR_UNSUPPORTED;

@@ -109,8 +109,8 @@ typedef struct {
 } eqattn_packing_t;
 
 /* Create a plan for `heads` query heads on `kv_heads` key/value heads of `dim`
- * values.  dim is a multiple of 8 up to EQATTN_MAX_DIM.  scale is finite and
- * positive.  buckets = 0 is a plan without a bias (span must be 0); otherwise
+ * values.  dim is a multiple of 8 up to EQATTN_MAX_DIM.  scale is positive and
+ * finite in binary32.  buckets = 0 is a plan without a bias (span must be 0); otherwise
  * offsets are clamped to [-span, span], 0 <= span <= EQATTN_MAX_SPAN, and the
  * table has `buckets` <= 65536 rows.  EQL_ERR_INVALID_ARG: heads, kv_heads, dim,
  * buckets or span negative (or 0 where at least 1 is needed), scale, heads not a

@@ -46,3 +46,11 @@ def test_no_key_value_heads_are_refused():
         AttnPlan(4, 64, kv_heads=0)
     plan = AttnPlan(4, 64)
     assert plan.Hk == 4
+
+
+@pytest.mark.parametrize("scale", [1e39, 1e300])
+def test_scales_beyond_binary32_are_refused(scale):
+    # they would be an infinity in every score
+    with pytest.raises(EqlinearError, match="EQL_ERR_INVALID_ARG"):
+        AttnPlan(4, 64, scale=scale)
+    AttnPlan(4, 64, scale=3e38)
