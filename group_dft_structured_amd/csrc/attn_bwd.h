@@ -57,22 +57,26 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(BwdWave
   if (!locate(c, w)) return;
   const int head = w.hk * c.G + w.rest % c.G, tile = a.tiles - 1 - w.rest / c.G;
   const int width = 2 * c.span + 1;
-  float* hist_out = nullptr;
-  if constexpr (BIAS != BIAS_NONE) {
-    if (a.hist != nullptr)
-      hist_out = a.hist + (((int64_t)w.seq * a.tiles + tile) * c.H + head) * width;
-  }
 
   int q0, lq, k0, lk;
   bounds(c.cu_q, w.seq, c.total_q, q0, lq);
   bounds(c.cu_k, w.seq, c.total_k, k0, lk);
   const int r0 = tile * ROWS;
   const int rows = lq - r0 < ROWS ? lq - r0 : ROWS;
-  if (rows <= 0) {
-    if (hist_out != nullptr)
-      for (int i = threadIdx.x; i < width; i += NT) hist_out[i] = 0.f;
-    return;
+  float* hist_out = nullptr;
+  if constexpr (BIAS != BIAS_NONE) {
+    if (a.hist != nullptr) {
+      // the tile's slot; the last tile, or the first one of an empty sequence, clears
+      // the slot behind it that is no other's
+      const int64_t slot = (int64_t)(q0 / ROWS) + w.seq + tile, pitch = (int64_t)c.H * width;
+      hist_out = a.hist + slot * pitch + (int64_t)head * width;
+      const bool first = tile == 0 && lq == 0, last = rows > 0 && r0 + ROWS >= lq;
+      const int64_t next = slot + (last ? 1 : 0);
+      if ((first || last) && next < (int64_t)((q0 + lq) / ROWS) + w.seq + 1)
+        for (int i = threadIdx.x; i < width; i += NT) a.hist[next * pitch + (int64_t)head * width + i] = 0.f;
+    }
   }
+  if (rows <= 0) return;
   const int shift = lk - lq;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int lane = threadIdx.x & 63, h = lane >> 5;

@@ -175,8 +175,15 @@ size_t delta_bytes(const eqattn_plan* p, const eqattn_packing_t* b) {
   return ru256((size_t)p->H * (size_t)b->total_q * sizeof(float));
 }
 
+// Parts of the sums over offsets.  Tile t of sequence b has slot
+// cu_q[b] / rows + b + t: a sequence's next slot is at most two behind its last, so
+// that there are total_q / rows + sequences of them whatever the longest sequence.
+// (One for every sequence and tile of the longest: 2 GiB for 256 sequences of 262144
+// tokens in all, the longest of 8192, 16 heads, span 1023; 300 MB so.)
 size_t hist_parts(const eqattn_packing_t* b, const BwdShape& s) {
-  return s.chunks > 0 ? (size_t)s.chunks : (size_t)b->sequences * s.tiles_q;
+  if (s.chunks > 0) return (size_t)s.chunks;
+  if (b->sequences == 0 || s.tiles_q == 0) return 0;
+  return (size_t)(b->total_q / (32 * s.waves_q) + b->sequences);
 }
 
 size_t hist_bytes(const eqattn_plan* p, const eqattn_packing_t* b, const BwdShape& s) {
@@ -328,9 +335,10 @@ eqlinear_status_t eqattn_backward(eqattn_plan_t p, const eqattn_packing_t* b,
   double* slices = (double*)((char*)hist + hist_bytes(p, b, s));
   a.hist = dtable != nullptr ? hist : nullptr;
   a.chunks = s.chunks;
+  a.c.slot_rows = s.chunks > 0 ? 0 : 32 * s.waves_q;
   if (b->sequences > 0) {
     Common probe = a.c;
-    if ((int64_t)hist_parts(b, s) > MAX_GRID || spread(probe, (int64_t)a.c.G * s.tiles_q, s.tiles_q == 1) < 0 ||
+    if (spread(probe, (int64_t)a.c.G * s.tiles_q, s.tiles_q == 1) < 0 ||
         spread(probe, s.tiles_k, s.tiles_k == 1) < 0)
       return EQL_ERR_UNSUPPORTED;
     st = hip_status("attention backward launch",

@@ -33,6 +33,7 @@ struct Common {
   const int32_t* map;
   // work-groups: per (sequence, key/value head) unit, and how units go to XCDs
   int per_unit, cluster, clusters, sorted;
+  int slot_rows;  // queries of a part of BwdArgs::hist; 0: a part is a chunk
 };
 
 struct FwdArgs {
@@ -49,7 +50,7 @@ struct BwdArgs {
   View dout, q, k, v, o, dq, dk, dv;
   const float* lse;
   float* delta;  // [H][total_q]
-  float* hist;   // [sequences][tiles] or [chunks], [H][2 span + 1]: partial sums of dtable, or nullptr
+  float* hist;   // [slots of tiles] or [chunks], [H][2 span + 1]: partial sums of dtable, or nullptr
   int tiles;
   int chunks;
 };

@@ -1,5 +1,6 @@
 // The bias table's gradient from the sums over offsets that the backward pass's
-// work-groups left: [parts][heads][2 span + 1], first over the parts, in a few
+// work-groups left: [parts][heads][2 span + 1], first over the parts (of the slots of
+// tiles, those up to the last sequence's end), in a few
 // slices, then over the slices and over the offsets of a bucket, in binary64: one
 // far bucket may hold most pairs of tokens, with both signs.  Fixed orders
 // throughout.  A few megabytes, bound by two launches: 5 + 7 us after the 258 us of
@@ -19,13 +20,22 @@ int slices_of(int parts) {
 }
 
 __global__ __launch_bounds__(1024) void k_bias_slices(const float* __restrict__ hist,
-                                                      double* __restrict__ slices, int parts, int cols) {
+                                                      double* __restrict__ slices, int parts, int cols,
+                                                      const int32_t* __restrict__ cu_q, int seqs,
+                                                      int total_q, int slot_rows) {
   __shared__ double s[16][64];
+  int first = 0;
+  if (slot_rows > 0 && parts > 0) {
+    const int start = cu_q[0], end = cu_q[seqs];
+    first = (start < 0 ? 0 : start > total_q ? total_q : start) / slot_rows;
+    const int behind = (end < 0 ? 0 : end > total_q ? total_q : end) / slot_rows + seqs;
+    parts = behind < parts ? behind : parts;
+  }
   const int col = blockIdx.x * 64 + (threadIdx.x & 63), sub = threadIdx.x >> 6;
   double v = 0.0;
   if (col < cols) {
 #pragma unroll 8
-    for (int p = blockIdx.y * 16 + sub; p < parts; p += 16 * gridDim.y) v += hist[(int64_t)p * cols + col];
+    for (int p = first + blockIdx.y * 16 + sub; p < parts; p += 16 * gridDim.y) v += hist[(int64_t)p * cols + col];
   }
   s[sub][threadIdx.x & 63] = v;
   __syncthreads();
@@ -71,7 +81,7 @@ hipError_t launch_bias_finish(const Common& c, const float* hist, int parts, dou
                               float* dtable, hipStream_t st) {
   const int width = 2 * c.span + 1, cols = c.H * width, count = slices_of(parts);
   hipLaunchKernelGGL(k_bias_slices, dim3((unsigned)((cols + 63) / 64), count), dim3(1024), 0, st, hist,
-                     slices, parts, cols);
+                     slices, parts, cols, c.cu_q, c.seqs, c.total_q, c.slot_rows);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(k_bias_buckets, dim3((unsigned)c.H, (unsigned)((c.buckets + 31) / 32)), dim3(256), 0, st, slices, c.map, dtable, c.H,

@@ -9,7 +9,7 @@ import pytest
 from tests import plain64
 from tests.attn_cases import make
 from tests.gpu_helpers import gpu_available, to_np64, torch_mod
-from tests.test_gpu_attention import U, _backward, _forward, _plain, _within
+from tests.test_gpu_attention import U, _backward, _forward, _packing, _plain, _plan, _within
 
 pytestmark = pytest.mark.gpu
 GRADS = ("dq", "dk", "dv", "dtable")
@@ -190,3 +190,47 @@ def test_queries_with_small_gradients_beside_large_ones(ratio, lens):
     assert np.isfinite(to_np64(grads[0])).all()
     everywhere = np.ones((sum(lens), 2), bool)
     _check_grads(c, grads, ref, mag, relative, rows=everywhere)
+
+
+# lengths whose tiles begin and end everywhere in the tiles of the packed tokens, with
+# sequences of no query among them
+RAGGED = [0, 1, 127, 128, 129, 0, 0, 300, 64, 255, 256, 257, 5, 0, 640, 33, 1, 0]
+
+
+@pytest.mark.parametrize("spare", [0, 1, 400])
+@pytest.mark.parametrize("bias", ["line", "grid"])
+@pytest.mark.parametrize("lens_q,Hk", [(RAGGED, 2), ([min(n, 64) for n in RAGGED], 1), ([0] * 6 + [130] + [0] * 5, 2)])
+def test_table_gradient_of_many_ragged_sequences(lens_q, Hk, bias, spare):
+    # spare: tokens after the last sequence; the workspace holds NaN before the call
+    torch = torch_mod()
+    c = make(lens_q, [n + 3 * (i % 2) for i, n in enumerate(lens_q)], 2, Hk, 16, "f32", bias == "line",
+             bias, seed=14, grid=23)
+    if bias == "grid":
+        rng = np.random.default_rng(3)
+        c["pos_q"] = np.concatenate([rng.permutation(676)[:n] for n in lens_q]).astype(np.int32)
+        c["pos_k"] = rng.integers(0, 676, c["k"].shape[0]).astype(np.int32)
+    plan, n = _plan(c), sum(lens_q)
+    o, lse = _forward(c)
+    want = to_np64(_backward(c, o, lse)[3])
+    longer = dict(c)
+    for name in ("q", "dout"):
+        longer[name] = np.concatenate([c[name], np.full((spare, 2, 16), 7, np.float32)])
+    if c["pos_q"] is not None:
+        longer["pos_q"] = np.concatenate([c["pos_q"], np.full(spare, 5, np.int32)])
+    ol = torch.full((n + spare, 2, 16), 7.0, device="cuda")
+    ol[:n] = o
+    ll = torch.full((2, n + spare), 7.0, device="cuda")
+    ll[:, :n] = lse
+    packing = _packing(longer)
+    ws = torch.full((plan.workspace_bytes(packing, n + spare, c["k"].shape[0])[1] // 4,), float("nan"),
+                    device="cuda")
+    dq = torch.full_like(ol, 7.0)
+    got = _backward(longer, ol, ll, plan, workspace=ws, dq=dq)
+    torch.cuda.synchronize()
+    ref, mag = plain64.attention_backward(c, c["dout"], c["q"], c["k"], c["v"], to_np64(o), to_np64(lse),
+                                          **_plain(c))
+    error = (c["dim"] + 8) * U * (_products(c) + np.abs(c["table"]).max())
+    _check_grads(c, [got[0][:n]] + list(got[1:]), ref, mag, 2 * error + 16 * U)
+    assert bool((dq[n:] == 7).all())
+    # the sums' places depend on the number of tokens at the end, their order does not
+    assert np.abs(to_np64(got[3]) - want).max() <= 2.0 ** -20 * np.abs(want).max()
