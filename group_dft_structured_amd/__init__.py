@@ -476,6 +476,7 @@ from .attention import (  # noqa: E402,F401
     Packing,
     eqattn_backward,
     eqattn_backward_workspace,
+    eqattn_backward_workspace_no_dtable,
     eqattn_forward,
     eqattn_forward_workspace,
     eqattn_plan_create,

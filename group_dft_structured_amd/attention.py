@@ -14,6 +14,7 @@ ATTN_EXPORTED = (
     "eqattn_forward_workspace",
     "eqattn_forward",
     "eqattn_backward_workspace",
+    "eqattn_backward_workspace_no_dtable",
     "eqattn_backward",
 )
 
@@ -46,6 +47,8 @@ def _lib():
     lib.eqattn_forward.restype = st
     lib.eqattn_backward_workspace.argtypes = [vp, pack]
     lib.eqattn_backward_workspace.restype = sz
+    lib.eqattn_backward_workspace_no_dtable.argtypes = [vp, pack]
+    lib.eqattn_backward_workspace_no_dtable.restype = sz
     lib.eqattn_backward.argtypes = [vp, pack] + [view] * 5 + [vp, vp, vp] + [view] * 3 + \
         [vp, vp, sz, vp]
     lib.eqattn_backward.restype = st
@@ -85,6 +88,10 @@ def eqattn_forward(plan, packing, q, k, v, table, bucket_map, o, lse, workspace,
 
 def eqattn_backward_workspace(plan, packing):
     return int(_lib().eqattn_backward_workspace(plan, _at(packing)))
+
+
+def eqattn_backward_workspace_no_dtable(plan, packing):
+    return int(_lib().eqattn_backward_workspace_no_dtable(plan, _at(packing)))
 
 
 def eqattn_backward(plan, packing, dout, q, k, v, o, lse, table, bucket_map, dq, dk, dv, dtable,
@@ -204,7 +211,7 @@ class AttnPlan:
         return o, lse
 
     def workspace_bytes(self, packing, total_q, total_k):
-        """(forward, backward) workspace bytes."""
+        """(forward, backward) workspace bytes, for a backward pass with dtable."""
         a = array("q", packing.fields(total_q, total_k, Launch(None)))
         pk = a.buffer_info()[0]
         return (eqattn_forward_workspace(self.handle, pk),
@@ -236,7 +243,8 @@ class AttnPlan:
         if workspace is not None:
             pw, nbytes = expect_workspace(workspace, dev)
         else:
-            nbytes = lib.eqattn_backward_workspace(self.handle, pk)
+            size = lib.eqattn_backward_workspace_no_dtable if pd is None else lib.eqattn_backward_workspace
+            nbytes = size(self.handle, pk)
             workspace = go.empty((nbytes,), go.torch.uint8)
             pw = workspace.data_ptr()
         st = lib.eqattn_backward(self.handle, pk, *views[:5], pl, pt, pm, *views[5:], pd, pw, nbytes,

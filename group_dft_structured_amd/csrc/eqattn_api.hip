@@ -298,6 +298,10 @@ size_t eqattn_backward_workspace(eqattn_plan_t p, const eqattn_packing_t* b) {
          (p->buckets > 0 ? slices_bytes(p) : 0);
 }
 
+size_t eqattn_backward_workspace_no_dtable(eqattn_plan_t p, const eqattn_packing_t* b) {
+  return p == nullptr || !sizes_ok(b) ? 0 : delta_bytes(p, b);
+}
+
 eqlinear_status_t eqattn_backward(eqattn_plan_t p, const eqattn_packing_t* b,
                                   const eqattn_view_t* dout, const eqattn_view_t* q,
                                   const eqattn_view_t* k, const eqattn_view_t* v,
@@ -325,7 +329,8 @@ eqlinear_status_t eqattn_backward(eqattn_plan_t p, const eqattn_packing_t* b,
   if ((b->total_q > 0 && lse == nullptr) || (p->buckets == 0 && dtable != nullptr))
     return EQL_ERR_INVALID_ARG;
   if (!aligned16(lse) || !aligned16(dtable) || !aligned16(workspace)) return EQL_ERR_MISALIGNED;
-  const size_t need = eqattn_backward_workspace(p, b);
+  const size_t need =
+      dtable != nullptr ? eqattn_backward_workspace(p, b) : eqattn_backward_workspace_no_dtable(p, b);
   if (need > 0 && (workspace == nullptr || workspace_bytes < need)) return EQL_ERR_WORKSPACE;
   const BwdShape s = backward_shape(p, b);
   fill_common(&a.c, p, b, table, map);

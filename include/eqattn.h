@@ -139,8 +139,12 @@ eqlinear_status_t eqattn_forward(eqattn_plan_t plan, const eqattn_packing_t* pac
                                  size_t workspace_bytes, void* stream);
 
 /* Bytes of device workspace eqattn_backward needs (0 for invalid arguments):
- * delta of every query row, and the partial sums of dtable. */
+ * delta of every query row, and the partial sums of dtable: about
+ * heads * (2 span + 1) * 4 bytes for every 64 or 128 queries and every sequence. */
 size_t eqattn_backward_workspace(eqattn_plan_t plan, const eqattn_packing_t* packing);
+
+/* The same where dtable is NULL: delta alone. */
+size_t eqattn_backward_workspace_no_dtable(eqattn_plan_t plan, const eqattn_packing_t* packing);
 
 /* dq, dk, dv and dtable (NULL = not wanted; NULL for a plan without a bias) from
  * the forward pass's inputs, its o and lse, and dout, the gradient of o.

@@ -32,3 +32,26 @@ def test_sums_over_offsets_follow_the_tokens(lib, seqs, tokens, heads, dim, span
         sizes.append(lib.eqattn_backward_workspace(plan, ctypes.addressof(packing)))
     eq.eqattn_plan_destroy(plan)
     assert all(0 < s <= most for s in sizes), (sizes, most)
+
+
+@pytest.mark.parametrize("buckets,span", [(0, 0), (8, 1000)])
+def test_a_call_without_dtable_needs_no_place_for_its_sums(lib, buckets, span):
+    # no sequence: arguments are checked, nothing is launched
+    heads, tokens = 6, 100
+    plan = eq.eqattn_plan_create(heads, heads, 64, 0.125, False, buckets, span, eq.EQL_F16)
+    packing = PackingStruct(0, tokens, tokens, 90, 90, None, None, None, None)
+    view = attention.View(A, 64 * heads, 64)
+    p, v, bias = ctypes.addressof(packing), ctypes.addressof(view), A if buckets else None
+    need = heads * tokens * 4  # delta
+
+    def call(nbytes, dtable=None):
+        return lib.eqattn_backward(plan, p, v, v, v, v, v, A, bias, bias, v, v, v, dtable, A, nbytes, None)
+
+    got = lib.eqattn_backward_workspace_no_dtable(plan, p)
+    assert need <= got < need + 256 and lib.eqattn_backward_workspace_no_dtable(plan, None) == 0
+    assert call(got) == 0 and call(got - 1) == 5
+    full = lib.eqattn_backward_workspace(plan, p)
+    assert full == got if buckets == 0 else full > got
+    if buckets:
+        assert call(full - 1, A) == 5
+    eq.eqattn_plan_destroy(plan)
