@@ -456,13 +456,6 @@ __global__ __launch_bounds__(64 * KW * QW) __attribute__((amdgpu_waves_per_eu(HD
   }
 }
 
-template <typename K>
-hipError_t allow_lds(K kernel, size_t lds) {
-  if (lds <= 65536) return hipSuccess;
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-}
-
 template <typename T, int HD, int NW, int BIAS>
 hipError_t run_bwd_q(const BwdArgs& a, int64_t grid, hipStream_t st) {
   typedef BwdLds<T, HD, NW> Lds;

@@ -476,6 +476,17 @@ __device__ __forceinline__ void store_rows(char* scratch, char* out, int64_t ts,
   wave_order();
 }
 
+// Lets a kernel have more than 64 KB of LDS.  Always the same number, a work-group's
+// most: the attribute belongs to the kernel, not to the call, and calls of several
+// threads set it with sizes of their own in mind.
+constexpr int LDS_BYTES = 163840;
+template <typename K>
+hipError_t allow_lds(K kernel, size_t lds) {
+  if (lds <= 65536) return hipSuccess;
+  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
+                             hipFuncAttributeMaxDynamicSharedMemorySize, LDS_BYTES);
+}
+
 __device__ __forceinline__ floatx16 zero16() {
   floatx16 z;
 #pragma unroll

@@ -335,11 +335,8 @@ hipError_t run_fwd(const FwdArgs& a, int64_t grid, hipStream_t st) {
   const size_t lds = Lds::TILES + (BIAS == BIAS_POSITIONS ? Lds::POS : 0) +
                      (BIAS == BIAS_NONE ? 0 : (size_t)(a.packed ? a.c.G : 1) * bias_width<BIAS>(a.c.span) * 4);
   const auto kernel = k_attn_fwd<T, HD, NW, BIAS>;
-  if (lds > 65536) {
-    const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-    if (e != hipSuccess) return e;
-  }
+  const hipError_t e = allow_lds(kernel, lds);
+  if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kernel, dim3((unsigned)grid), dim3(64 * NW), lds, st, a);
   return hipGetLastError();
 }

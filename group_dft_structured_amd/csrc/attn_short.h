@@ -457,13 +457,6 @@ __global__ __launch_bounds__(128) __attribute__((amdgpu_waves_per_eu(HD * sizeof
   }
 }
 
-template <typename K>
-hipError_t short_lds(K kernel, size_t lds) {
-  if (lds <= 65536) return hipSuccess;
-  return hipFuncSetAttribute(reinterpret_cast<const void*>(kernel),
-                             hipFuncAttributeMaxDynamicSharedMemorySize, (int)lds);
-}
-
 template <typename T, int HD, int BIAS>
 hipError_t run_short_fwd(const FwdArgs& a, unsigned grid, hipStream_t st) {
   const size_t lds = 4 * Tile<T, HD, SHORT>::BYTES + SHORT * 4 + (size_t)(2 * a.c.span + 1) * 4;
@@ -478,7 +471,7 @@ hipError_t run_short_bwd(const BwdArgs& a, unsigned grid, hipStream_t st) {
   const size_t lds = 4 * Tile<T, HD, SHORT>::BYTES + 2 * Tile<T, SHORT, SHORT>::BYTES + 7 * SHORT * 4 + 4 * 8 +
                      (BIAS == BIAS_NONE ? 0 : width * 4 + (a.hist != nullptr ? 4 * (width + 1) * 4 : 0));
   const auto kernel = k_attn_short_bwd<T, HD, BIAS>;
-  const hipError_t e = short_lds(kernel, lds);
+  const hipError_t e = allow_lds(kernel, lds);
   if (e != hipSuccess) return e;
   hipLaunchKernelGGL(kernel, dim3(grid), dim3(128), lds, st, a);
   return hipGetLastError();
