@@ -154,21 +154,21 @@ __device__ __forceinline__ u32x4 load16(Buffer b, uint32_t off) {
 template <typename T, int HD, int NT, int R = Tile<T, HD>::ROWS>
 struct Stage {
   typedef Tile<T, HD, R> Tl;
-  static constexpr bool IDLE = Tl::ROWS * Tl::CPR < NT;  // fewer chunks than threads
-  static constexpr int N = IDLE ? 1 : Tl::ROWS * Tl::CPR / NT, STEP = NT / Tl::CPR;
+  static constexpr int N = Tl::ROWS * Tl::CPR / NT, STEP = NT / Tl::CPR;
+  static_assert(N > 0 && Tl::ROWS * Tl::CPR % NT == 0 && NT % Tl::CPR == 0,
+                "every thread takes the same chunk of N rows");
   u32x4 r[N];
   __device__ __forceinline__ void load(const char* base, int64_t ts, int left, int dim,
                                        int tid = threadIdx.x) {
     const int row = tid / Tl::CPR, ch = tid % Tl::CPR;
     const Buffer b = rows_of<T>(base, left < R ? left : R, ts, dim);
     const uint32_t pitch = (uint32_t)ts * Tl::ES;
-    const uint32_t off = ch * Tl::EPC < dim && (!IDLE || row < R) ? row * pitch + ch * 16 : NO_ROW;
+    const uint32_t off = ch * Tl::EPC < dim ? row * pitch + ch * 16 : NO_ROW;
 #pragma unroll
     for (int n = 0; n < N; ++n) r[n] = load16(b, off + n * (STEP * pitch));
   }
   __device__ __forceinline__ void store(char* lds, int tid = threadIdx.x) const {
     const int row = tid / Tl::CPR, ch = tid % Tl::CPR;
-    if (IDLE && row >= R) return;
 #pragma unroll
     for (int n = 0; n < N; ++n)
       *reinterpret_cast<u32x4*>(lds + Tl::at(row + n * STEP, ch)) = r[n];
@@ -194,16 +194,6 @@ struct RowFrag {
       else
         c[s] = u32x4{0, 0, 0, 0};
     }
-  }
-  // row row0 + l % 32 of `rows` rows of a tensor; zeros behind
-  __device__ __forceinline__ void load(const char* base, int64_t ts, int row0, int rows, int dim) {
-    typedef Tile<T, HD> Tl;
-    const int lane = threadIdx.x & 63;
-    const Buffer b = rows_of<T>(base, rows, ts, dim);
-    const uint32_t off = (row0 + (lane & 31)) * ((uint32_t)ts * Tl::ES) + (lane >> 5) * 16;
-#pragma unroll
-    for (int s = 0; s < Tl::STEPS; ++s)
-      c[s] = load16(b, (2 * s + (lane >> 5)) * Tl::EPC < dim ? off + 32 * s : NO_ROW);
   }
   // row row0 + l % 32 of a tile in LDS
   __device__ __forceinline__ void read(const char* tile, int row0, int tid = threadIdx.x) {
