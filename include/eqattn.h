@@ -64,10 +64,15 @@
  *     dtable : [buckets][H] binary32
  *     cu_q, cu_k : [sequences + 1] int32, token offsets, non-decreasing from 0
  *     pos_q : [total_q] int32, pos_k : [total_k] int32 (both or neither NULL)
- * Offsets are read on the GPU; they are clamped to the token counts, and only
- * the first max_q queries and max_k keys of a sequence have outputs written.
- * Outputs of tokens that belong to no sequence are left alone.  Positions and
- * their differences must stay within 31 bits.
+ * Offsets are read on the GPU and clamped to the token counts.  A sequence longer
+ * than max_q or max_k says, or offsets that decrease, give unspecified outputs, inside
+ * the tensors.  Outputs of tokens that belong to no sequence are left alone.
+ * Positions and their differences must stay within 31 bits.
+ *
+ * Caches with room behind their tokens: the room is a sequence of its own without
+ * queries, so that cu_k is 0, len0, room, room + len1, 2 room, ... and cu_q 0, 1, 1,
+ * 2, 2, ...  (Keys are split over work-groups by the number of sequences, these
+ * among them: half as many pieces as packed caches get.)
  *
  * Ownership, streams, errors and concurrency are as in eqlinear.h: buffers
  * belong to the caller, every call is asynchronous on the given HIP stream,

@@ -234,3 +234,26 @@ def test_table_gradient_of_many_ragged_sequences(lens_q, Hk, bias, spare):
     assert bool((dq[n:] == 7).all())
     # the sums' places depend on the number of tokens at the end, their order does not
     assert np.abs(to_np64(got[3]) - want).max() <= 2.0 ** -20 * np.abs(want).max()
+
+
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+@pytest.mark.parametrize("lens,room", [([30, 64, 1], 100), ([700, 1500, 2100], 2500)])
+def test_caches_with_spare_room(lens, room, dtype):
+    # the room behind a cache's tokens is a sequence of its own without queries
+    torch = torch_mod()
+    c = make([1] * 3, lens, 8, 2, 64, dtype, True, "line", seed=15)
+    want = _forward(c)
+    d = dict(c, max_k=room)
+    for name in ("k", "v"):
+        d[name] = np.full((3 * room, 2, 64), np.nan, c[name].dtype)
+        for i, n in enumerate(lens):
+            d[name][i * room:i * room + n] = c[name][sum(lens[:i]):sum(lens[:i + 1])]
+    d["cu_q"] = np.array([0, 1, 1, 2, 2, 3, 3], np.int32)
+    d["cu_k"] = np.array([0] + [x for i, n in enumerate(lens) for x in (i * room + n, (i + 1) * room)], np.int32)
+    got = _forward(d)
+    torch.cuda.synchronize()
+    # sums of other pieces of the keys (none of the short caches)
+    error = (2.0 ** -10 if dtype == "f16" else 0) + (max(lens) + 64) * U
+    mag = plain64.attention(c, c["q"], c["k"], np.abs(c["v"]), **_plain(c))[0]
+    assert (np.abs(to_np64(got[0]) - to_np64(want[0])) <= error * mag + 2.0 ** -24).all()
+    assert np.abs(to_np64(got[1]) - to_np64(want[1])).max() <= (max(lens) + 64) * U + 8 * U * 20
