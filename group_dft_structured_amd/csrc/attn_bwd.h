@@ -12,13 +12,14 @@
 //
 // The sums over offsets: attn_sums.h.
 //
-// Measured: 16 packed documents of 33 to 2048 tokens, 12 heads of 64 on 4, causal
-// with a bias, binary16: 120 us queries (75 us without the bias: its sums, and LDS
-// for two work-groups a compute unit where three would run) + 138 us keys; 67.5
-// GFLOP of five products, 94.5 of the seven: 370 TFLOP/s.  16 full sequences of
-// 2048: 570 TFLOP/s (five products), causal 444.  64 images of 197 tokens, 6 heads
-// of 64, binary32: 87 + 112 us (9.5 GFLOP of five products, 20 of seven on 197
-// tokens padded to 224 queries or 256 keys: 100 TFLOP/s of 152 by the matrix cores).
+// Measured (kernel times, steady state): 16 packed documents of 33 to 2048 tokens, 12
+// heads of 64 on 4, causal with a bias, binary16: 110 us queries (76 us without the
+// bias: its sums, and LDS for two work-groups a compute unit where three would run) +
+// 126 us keys (118); 67.5 GFLOP of five products, 94.5 of the seven: 400 TFLOP/s.  16
+// full sequences of 2048: 570 TFLOP/s (five products), causal 420.  64 images of 197
+// tokens, 6 heads of 64, binary32: 80 + 102 us (9.5 GFLOP of five products, 20 of seven
+// on 197 tokens padded to 224 queries or 256 keys: 110 TFLOP/s of 152 by the matrix
+// cores).
 #pragma once
 
 #include "attn_device.h"

@@ -41,7 +41,7 @@ enum { BIAS_NONE = 0, BIAS_INDEX = 1, BIAS_POSITIONS = 2 };
 // which read the same keys and values (or, for heads shorter than a cache line,
 // the same lines), are those of one XCD, one cluster after the other.  (All
 // clusters' largest pieces of work first balances better, but the keys and values
-// of many units do not stay in one L2: 190 us for 173 us on packed prompts.)
+// of many units do not stay in one L2: 10% more time on packed prompts.)
 struct Where {
   int seq, hk, rest;
 };

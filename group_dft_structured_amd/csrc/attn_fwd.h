@@ -20,13 +20,14 @@
 //
 // Tiles of 64 keys in binary16: two blocks of scores in flight a wave hide each
 // other's exponentials; four waves share a tile, so LDS is read once a 128 queries.
-// Measured, binary16: 12 packed prompts of 65 to 2048 tokens, 16 heads of 128 on 4,
-// causal with a bias, 138 us (76.7 GFLOP: 560 TFLOP/s; 16 full sequences of 2048
-// run at 850 TFLOP/s, causal 600): what lacks are the start of a work-group (queries,
-// first tile, bias: 9 us with its end) and the unequal lengths.  One token for 48
-// caches of up to 8192, 32 heads of 128 on 8: 166 + 6 us (817 MB: 4.8 TB/s, near a
-// copy's 5.1).  One token for one cache of 32768, 16 heads of 64 on 4: 10.5 + 6 us
-// (33.6 MB from the memory-side cache; two launches' starts).
+// Measured (kernel times, steady state), binary16: 12 packed prompts of 65 to 2048
+// tokens, 16 heads of 128 on 4, causal with a bias, 132 us, 126 without the bias (76.7
+// GFLOP: 580 TFLOP/s; 16 full sequences of 2048 run at 860 TFLOP/s, causal 760): what
+// lacks are the start of a work-group (queries, first tile, bias: 9 us with its end)
+// and the unequal lengths.  Binary32: 900 us.  One token for 48 caches of up to 8192,
+// 32 heads of 128 on 8: 165 + 6 us (817 MB: 4.9 TB/s, near a copy's 5.1); binary32 300 +
+// 6 us (5.4 TB/s).  One token for one cache of 32768, 16 heads of 64 on 4: 11 + 6 us
+// (33.6 MB from the memory-side cache; two launches' starts); binary32 27 + 5 us.
 #pragma once
 
 #include "attn_device.h"
@@ -47,7 +48,7 @@ struct FwdLds {
 // wave the products' results go to accumulation registers and are moved back).
 // Two waves a work-group hold twice the next tile's rows each: one wave a SIMD
 // fewer from dimension 64 on, where they would need scratch memory (512 sequences
-// of 40 to 64 tokens, 8 heads of 128 on 2: 67 us for 70 us).
+// of 40 to 64 tokens, 8 heads of 128 on 2: 4% less time).
 template <typename T, int HD, int NW>
 struct FwdWaves {
   static constexpr int f16 = (HD == 32 ? 4 : HD == 64 ? 3 : 2) - (NW == 2 && HD >= 64 ? 1 : 0);

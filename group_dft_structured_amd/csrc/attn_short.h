@@ -13,9 +13,10 @@
 // computes every score once: a wave takes 32 queries against all keys (dq, and p
 // and ds to LDS), then 32 keys against all queries (dk and dv from p and ds).
 //
-// Measured, 4096 windows of 49 tokens, 6 heads of 32, bias over the grid, binary16:
-// forward 71 us (313 MB: 4.4 TB/s; the long kernel 160 us), backward 180 us (621 MB:
-// 3.4 TB/s; the long passes 490 us).  The forward pass is bound by its loads and
+// Measured (kernel times, steady state), 4096 windows of 49 tokens, 6 heads of 32, bias
+// over the grid, binary16: forward 71 us (313 MB: 4.4 TB/s; the long kernel 160 us),
+// backward 174 us (621 MB: 3.6 TB/s; the long passes 490 us); binary32 163 us and 539
+// us (two work-groups a compute unit by their LDS).  The forward pass is bound by its loads and
 // stores of 64 bytes a row and head; the backward pass by the instructions around
 // its small products: 49 tokens fill 59% of a 64 x 64 tile.  Four waves of 32 x 32
 // scores, with four barriers a sequence instead of three: 201 us.

@@ -106,7 +106,9 @@ namespace attn {
 // 4096 windows took 102 us for 90 us forward and 231 us for 203 us backward).  They
 // go round the XCDs, so that it is an XCD's 32 compute units that hold them: six
 // heads on two places, 84 work-groups a head, left two of 66 waiting on half of the
-// XCDs (877 us for 559 us, binary32 backward).
+// XCDs (877 us for 559 us, binary32 backward).  Shared key/value heads and wider rows
+// take the long kernels: the same windows with 6 heads on 3 take 88 us forward and
+// 383 us backward for 76 us and 183 us.
 int short_chunks(const eqattn_plan* p, const eqattn_packing_t* b, int places) {
   if (p->H != p->Hk || p->dim * p->esize > 128 || max_q_of(b) > 64 || max_k_of(b) > 64) return 0;
   const int64_t an_xcd = 32 * places / p->H, most = 8 * (an_xcd < 1 ? 1 : an_xcd);
@@ -200,7 +202,8 @@ int64_t spread(Common& c, int64_t per_unit, bool one_tile) {
   // a time.
   c.cluster = one_tile && c.dim * c.esize < 128 ? c.Hk : 1;
   const int64_t clusters = units / c.cluster;
-  // lengths that differ: the mean at most nine tenths of the longest
+  // lengths that differ: the mean at most nine tenths of the longest (up to 64
+  // sequences, a lane each; more of them go in the order given)
   c.sorted = per_unit > 1 && c.seqs > 1 && c.seqs <= 64 &&
              (int64_t)c.total_k * 10 < (int64_t)c.seqs * c.max_k * 9;
   if (clusters < 32 && clusters % 8 != 0) {

@@ -14,8 +14,11 @@ struct eqnorm_plan {
 namespace eql {
 
 // Most work-groups of a pass: those that find a place on the chip at once, five a
-// compute unit forward and three backward (by their registers at three vectors a
-// lane).
+// compute unit forward and three backward, by their registers at three vectors of
+// binary16 a lane (384 and 768 features, where it was measured).  Other widths find
+// other numbers of places, so that their last turn may be a part of one: at four
+// vectors a lane (1024, 4096 features) four a compute unit forward and two backward,
+// two backward in binary32 at three vectors, and two or one above 4096 features.
 constexpr int64_t FWD_BLOCKS = 1280, BWD_BLOCKS = 768;
 
 // Work-groups, and so partial sums, of a backward pass over N rows.

@@ -19,10 +19,12 @@
 // a second launch adds the partials, again in a fixed order (atomics would make
 // the last bits depend on timing).
 //
-// Measured, binary16 (kernel times): 12608 rows of 384 forward 8.8 us (19.5 MB) and
-// backward 12.3 + 3.9 us (29.2 MB), where the operands sit in the memory-side cache
-// and a launch's start and end are half the time; 200704 rows of 768 backward
-// 166 + 5 us (926 MB: 5.4 TB/s, the rate of a large copy).
+// Measured (kernel times, steady state), binary16: 12608 rows of 384 forward 8.4 us
+// (19.5 MB) and backward 12.1 + 3.8 us (29.2 MB) from the memory-side cache, where 64
+// rows take 2.4 us: 10.4 and 20.0 + 3.8 us in binary32; 200704 rows of 768 backward 166 +
+// 5 us (926 MB: 5.4 TB/s, the rate of a large copy), binary32 348 + 5 us.  12608 rows of
+// 4096: 49 us forward (4.3 TB/s), 62 + 5 us backward (5.0 TB/s).  Above 8192 features the
+// backward pass does not fit the registers (4096 rows of 16384: 207 + 6 us, 1.9 TB/s).
 #include <type_traits>
 
 #include "eqnorm_internal.h"

@@ -50,7 +50,8 @@
 extern "C" {
 #endif
 
-/* Most features C * T of a row: a row is kept in the registers of one work-group. */
+/* Most features C * T of a row: a row is kept by one work-group, in registers up to
+ * 8192 features and partly in scratch memory backward above. */
 #define EQNORM_MAX_FEATURES 16384
 
 typedef struct eqnorm_plan* eqnorm_plan_t; /* opaque */
