@@ -1,6 +1,6 @@
 // C ABI of the norm (include/eqnorm.h): argument validation and dispatch.
 // Every check runs before the first HIP call.
-#include <math.h>
+#include <float.h>
 #include <string.h>
 
 #include <new>
@@ -28,7 +28,7 @@ eqlinear_status_t eqnorm_plan_create(int64_t C, int64_t T, double eps, eqlinear_
                                      eqnorm_plan_t* out) {
   if (out == nullptr) return EQL_ERR_INVALID_ARG;
   *out = nullptr;
-  if (C <= 0 || !isfinite(eps) || eps < 0) return EQL_ERR_INVALID_ARG;
+  if (C <= 0 || !(eps >= 0 && eps <= FLT_MAX) || (eps > 0 && (float)eps == 0.f)) return EQL_ERR_INVALID_ARG;
   const int dv = eql::enum_value(dtype_arg);
   if (dv != EQL_F32 && dv != EQL_F16) return EQL_ERR_UNSUPPORTED;
   if (T < 1 || T > MAX_T || C > EQNORM_MAX_FEATURES / T) return EQL_ERR_UNSUPPORTED;

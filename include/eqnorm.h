@@ -57,7 +57,8 @@ extern "C" {
 typedef struct eqnorm_plan* eqnorm_plan_t; /* opaque */
 
 /* Create a plan for rows of C channels of T group values, 1 <= T <= 16.
- * EQL_ERR_INVALID_ARG: C <= 0, eps negative or not finite, out == NULL;
+ * EQL_ERR_INVALID_ARG: C <= 0, eps negative or not finite or (unless 0) outside
+ * binary32, out == NULL;
  * EQL_ERR_UNSUPPORTED: T or dtype out of range, C * T > EQNORM_MAX_FEATURES.
  * Host-only: allocates no device memory. */
 eqlinear_status_t eqnorm_plan_create(int64_t C, int64_t T, double eps, eqlinear_dtype_t dtype,
